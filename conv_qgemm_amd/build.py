@@ -42,8 +42,10 @@ CFLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     f"-I{os.path.join(ROOT, 'include')}",
 ]
-# Per-source additions.  The attention kernels meet no NaN (masked scores are
-# -infinity): without that promise every maximum first re-rounds its operands.
+# Per-source additions.  The attention kernels make no NaN from the finite
+# values that they take (masked scores are -infinity and never meet a factor of
+# 0, scales of 0 are held above it: attn_weights.hpp): without that promise
+# every maximum first re-rounds its operands.
 # The large-GEMM ring keeps its 256 accumulators of
 # 16x16 MFMA tiles in place only when the pre-RA machine scheduler is off:
 # with it, the compiler reorders the loop's MFMAs so that about half of them

@@ -21,6 +21,8 @@
 #include <type_traits>
 
 #include "kv_common.hpp"
+
+#include "attn_weights.hpp"
 #include "launch.hpp"
 
 namespace qg {
@@ -318,7 +320,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_rows16(AttnArgs 
     constexpr int KS = D / 32;   // MFMA steps over d
     constexpr int VD = D / 16;   // values per lane and token, and 16-row tiles of out^T
     constexpr int VW = VD / 4;   // dwords of them
-    constexpr float kLift = 6.0f;   // weights are 2^6 times larger: small ones keep bits
     constexpr float kSlack = 8.0f;  // a maximum may lag by 2^8 before the sums are rescaled
     const AttnDesc &d = a.d;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -384,7 +385,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_rows16(AttnArgs 
 #pragma unroll
     for (int t = 0; t < VD; ++t)
         o[t] = (v4f){0, 0, 0, 0};
-    float m = -INFINITY, l = 0.0f, R = 0.0f, log2R = 0.0f;
+    float m = kNothing, l = 0.0f, R = 0.0f, log2R = 0.0f;
 
     // a tile's four runs of 16 tokens; runs past the last token re-read the
     // last one (its weights are masked).  Lane 4 k + s looks after run s.
@@ -439,8 +440,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_rows16(AttnArgs 
         float mt = -INFINITY, kc[4], vs[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            kc[s] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(tl.ks), s)) * a.c2;
-            vs[s] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(tl.vs), s));
+            kc[s] = score_factor(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(tl.ks), s)), a.c2);
+            vs[s] = held_scale(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(tl.vs), s)));
             x[s] = (v4f){0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
@@ -457,12 +458,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_rows16(AttnArgs 
                     x[s][e] = j0 + e < sees ? x[s][e] : -INFINITY;
             }
             float mu = fmaxf(fmaxf(x[s][0], x[s][1]), fmaxf(x[s][2], x[s][3]));
-            // a scale of 0 would turn -inf into NaN
-            if constexpr (MASKED)
-                mu = mu == -INFINITY ? mu : mu * kc[s];
-            else
-                mu *= kc[s];
-            mt = fmaxf(mt, mu);
+            mt = fmaxf(mt, mu * kc[s]);
         }
         const auto s16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(mt), __float_as_uint(mt), false, false);
         mt = fmaxf(__uint_as_float(s16[0]), __uint_as_float(s16[1]));
@@ -490,21 +486,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_rows16(AttnArgs 
                 for (int e = 0; e < 4; ++e)
                     o[t][e] *= shrink;
         }
-        const float mz = MASKED && m == -INFINITY ? 0.0f : m;
         v4i wf[2], wr[2];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            // weights take 2^b (value scale / R, lifted), sums take it back; a
-            // block of zeros has scale 0, whose weights vanish harmlessly
-            const float lv = fmaxf(__builtin_amdgcn_logf(vs[s]) - log2R, -80.0f) + kLift;
-            const float back = fminf(R * __builtin_amdgcn_rcpf(vs[s]), 0x1p80f) * 0x1p-6f;
+            // weights take 2^lv (value scale / R, lifted), sums take it back
+            const float lv = run_shift(__builtin_amdgcn_logf(vs[s]), log2R);
+            const float back = run_back(R, __builtin_amdgcn_rcpf(vs[s]));
             float p[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[s][e], kc[s], lv - mz));
-                if constexpr (MASKED)
-                    p[e] = x[s][e] == -INFINITY ? 0.0f : p[e];
-            }
+            for (int e = 0; e < 4; ++e)
+                p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[s][e], kc[s], lv - m));
             l = __builtin_fmaf((p[0] + p[1]) + (p[2] + p[3]), back, l);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -586,12 +577,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_rows16(AttnArgs 
         if (row0 + r >= n * G)
             break;
         float mm = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
-        const float mz = mm == -INFINITY ? 0.0f : mm;
         float ll = 0.0f;
         v4f oo = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
-            const float e2 = __builtin_amdgcn_exp2f(sm[w][r] - mz);
+            const float e2 = __builtin_amdgcn_exp2f(sm[w][r] - mm);
             ll = __builtin_fmaf(e2, sl[w][r], ll);
             const v4f x = *(const v4f *)&so[w][r][c];
             for (int e = 0; e < 4; ++e)
@@ -750,9 +740,10 @@ struct Widen {
             }
         }
         // every wave of a run writes the same scales
+        const float sv = held_scale(scale_v);
         if (lane == 0)
-            *(v4f *)(scl + 4 * run) = (v4f){scale_k * a.c2, scale_v, __builtin_amdgcn_logf(scale_v),
-                                            __builtin_amdgcn_rcpf(scale_v)};
+            *(v4f *)(scl + 4 * run) = (v4f){score_factor(scale_k, a.c2), sv, __builtin_amdgcn_logf(sv),
+                                            __builtin_amdgcn_rcpf(sv)};
     }
 };
 
@@ -815,7 +806,6 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(D, READY)) void k_attn_rows_m
     // takes its rest.  It costs a binary16 prompt of 8192 tokens 190 us, 837
     // instead of 647.
     constexpr bool REST = DT == DT_F16;
-    constexpr float kLift = 6.0f;   // weights are 2^6 times larger: small ones keep bits
     constexpr float kSlack = 8.0f;  // a maximum may lag by 2^8 before the sums are rescaled
     __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kBuf];
 
@@ -863,7 +853,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(D, READY)) void k_attn_rows_m
     for (int t = 0; t < DT32; ++t)
         for (int e = 0; e < 16; ++e)
             o[t][e] = 0.0f;
-    float m = -INFINITY, l = 0.0f, R = 0.0f, log2R = 0.0f;
+    float m = kNothing, l = 0.0f, R = 0.0f, log2R = 0.0f;
 
     // LDS offsets of this lane's fragments: chunk 2 s + h of row r32 (and of
     // rows 32, 64, .. further, which swizzle alike) is at place ^ 32 s
@@ -929,12 +919,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(D, READY)) void k_attn_rows_m
 #pragma unroll
             for (int e = 1; e < 8; ++e)
                 mu = fmaxf(mu, x[u >> 1][8 * (u & 1) + e]);
-            // a scale of 0 would turn -inf into NaN
-            if constexpr (MASKED)
-                mu = mu == -INFINITY ? mu : mu * sc[u][0];
-            else
-                mu *= sc[u][0];
-            mt = fmaxf(mt, mu);
+            mt = fmaxf(mt, mu * sc[u][0]);
         }
         const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mt), __float_as_uint(mt),
                                                          false, false);
@@ -955,21 +940,15 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(D, READY)) void k_attn_rows_m
                 for (int e = 0; e < 16; ++e)
                     o[t][e] *= shrink;
         }
-        const float mz = MASKED && m == -INFINITY ? 0.0f : m;
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            // weights take 2^b (value scale / R, lifted), sums take it back; a
-            // block of zeros has scale 0, whose weights vanish harmlessly
-            const float b = fmaxf(sc[u][2] - log2R, -80.0f) + kLift - mz;
-            const float back = fminf(sc[u][3] * R, 0x1p80f) * 0x1p-6f;
+            // weights take 2^b (value scale / R, lifted), sums take it back
+            const float b = run_shift(sc[u][2], log2R) - m;
+            const float back = run_back(R, sc[u][3]);
             float p[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float xv = x[u >> 1][8 * (u & 1) + e];
-                p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(xv, sc[u][0], b));
-                if constexpr (MASKED)
-                    p[e] = xv == -INFINITY ? 0.0f : p[e];
-            }
+            for (int e = 0; e < 8; ++e)
+                p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[u >> 1][8 * (u & 1) + e], sc[u][0], b));
             const float sum = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
             l = __builtin_fmaf(sum, back, l);
 #pragma unroll
@@ -1385,7 +1364,7 @@ hipError_t launch_attn_kv8(const AttnDesc &d, hipStream_t s)
     a.extra = 1;
     a.few = kFew;
     a.one_tile = p.top <= 16;
-    a.c2 = d.scale * kLog2e;
+    a.c2 = d.scale < 2.0e38f ? d.scale * kLog2e : 3.4e38f;  // finite
     a.block_shift = __builtin_ctz((unsigned)d.c.block_size);
     a.num_blocks = (unsigned)d.c.num_blocks;
     a.images = (uint8_t *)d.workspace;
