@@ -2,10 +2,10 @@
 // scores, softmax weights and their sum in attention over the int8 cache: plain
 // binary32 arithmetic that also builds for the host.
 //
-// Every factor here is finite and above 0 for every scale that a cache may
-// hold, 0 (a block of zeros) included, so that neither 0 * infinity nor
-// infinity - infinity occurs: the attention kernels are compiled on the promise
-// that no operation makes a NaN.
+// Every factor here is finite for every scale that a cache may hold, 0 (a block
+// of zeros) included, and scores' factors are above 0, so that neither 0 *
+// infinity nor infinity - infinity occurs: the attention kernels are compiled on
+// the promise that no operation makes a NaN.
 #pragma once
 
 namespace qg {
@@ -28,14 +28,16 @@ __device__ __forceinline__ float score_factor(float ks, float c2)
 
 __device__ __forceinline__ float held_scale(float s) { return __builtin_fmaxf(s, kLeastScale); }
 
-// log2 of the factor s / R of a weight, lifted.  Under 2^-80 it stays there: the
-// values vanish beside the others, but the sum still needs the weights.
+// log2 of the factor s / R of a weight, lifted (R: the row's largest weight
+// times scale).  Under 2^-80 it stays there: the values vanish beside the
+// others, but the sum still needs the weights.
 __device__ __forceinline__ float run_shift(float log2s, float log2R)
 {
     return __builtin_fmaxf(log2s - log2R, -80.0f) + kLift;
 }
 
-// What takes that factor out of the weight again, for the sum; rs = 1 / s.
+// What takes that factor out of the weight again, for the sum; rs = 1 / s.  It
+// may underflow: the row's weight is no more then.
 __device__ __forceinline__ float run_back(float R, float rs)
 {
     return __builtin_fminf(R * rs, 0x1p80f) * 0x1p-6f;

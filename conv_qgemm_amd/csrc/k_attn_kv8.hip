@@ -8,10 +8,13 @@
 // Codes times scales.  A code is exact in binary16 and in bfloat16, so keys
 // enter the matrix product as codes and a block's scale multiplies its
 // scores.  A block's value scale s joins the weight: the product takes
-// w_j = 2^(x_j - m + log2(s / R)) with codes, and l collects w_j * (R / s).
-// R, the same for all rows of a wave, is at least every value scale seen so
-// far, so w stays within [0, 1] and neither binary16's range nor bfloat16's
-// matters; when a larger scale comes, R doubles past it and the sums shrink.
+// w_j = 2^(x_j + log2 s_j - y) with codes, where y is the row's running maximum
+// of x_j + log2 s_j over the tokens that it sees, and l collects w_j * (R / s)
+// with R = 2^(y - m).  So w stays within [0, 1] and the row's largest term is
+// near 1: what a weight loses to binary16's range is small beside the row's own
+// terms, whatever scales other rows or hidden tokens have.  (One R for a wave,
+// at least every scale met, was as fast but let a row vanish beside a later
+// block's scale.)
 //
 // The product K Q^T leaves token x row tiles in the layout that the second
 // product, V^T W^T, takes its weights in (a lane holds 4 tokens of one row
@@ -161,10 +164,16 @@ __device__ __forceinline__ v4i widen_col(const int (&w)[8])
     return r;
 }
 
-template <int DT>
-__device__ __forceinline__ void store_elem(void *p, int64_t i, float x)
+// the larger of x in lanes that differ in bit 4, or bit 5, of their number
+__device__ __forceinline__ float max_of_16s(float x)
 {
-    ((uint16_t *)p)[i] = (uint16_t)pack2<DT>(x, x);
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float max_of_halves(float x)
+{
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
 }
 
 // Shares: sequences cut into parts of about one length, one workgroup for each,
@@ -385,7 +394,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_rows16(AttnArgs 
 #pragma unroll
     for (int t = 0; t < VD; ++t)
         o[t] = (v4f){0, 0, 0, 0};
-    float m = kNothing, l = 0.0f, R = 0.0f, log2R = 0.0f;
+    float m = kNothing, y = kNothing, l = 0.0f, R = 1.0f, log2R = 0.0f;
 
     // a tile's four runs of 16 tokens; runs past the last token re-read the
     // last one (its weights are masked).  Lane 4 k + s looks after run s.
@@ -437,11 +446,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_rows16(AttnArgs 
         constexpr bool MASKED = decltype(masked_tag)::value;
         // scores of 16 tokens x 16 rows: lane holds tokens 4 g + e of row r16
         v4f x[4];
-        float mt = -INFINITY, kc[4], vs[4];
+        float mt = -INFINITY, yt = -INFINITY, kc[4], vs[4], log2s[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             kc[s] = score_factor(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(tl.ks), s)), a.c2);
             vs[s] = held_scale(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(tl.vs), s)));
+            log2s[s] = __builtin_amdgcn_logf(vs[s]);
             x[s] = (v4f){0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
@@ -457,40 +467,31 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_rows16(AttnArgs 
                 for (int e = 0; e < 4; ++e)
                     x[s][e] = j0 + e < sees ? x[s][e] : -INFINITY;
             }
-            float mu = fmaxf(fmaxf(x[s][0], x[s][1]), fmaxf(x[s][2], x[s][3]));
+            const float mu = fmaxf(fmaxf(x[s][0], x[s][1]), fmaxf(x[s][2], x[s][3]));
             mt = fmaxf(mt, mu * kc[s]);
+            yt = fmaxf(yt, __builtin_fmaf(mu, kc[s], log2s[s]));
         }
-        const auto s16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(mt), __float_as_uint(mt), false, false);
-        mt = fmaxf(__uint_as_float(s16[0]), __uint_as_float(s16[1]));
-        const auto s32 = __builtin_amdgcn_permlane32_swap(__float_as_uint(mt), __float_as_uint(mt), false, false);
-        mt = fmaxf(__uint_as_float(s32[0]), __uint_as_float(s32[1]));
-        float shrink = 1.0f;
-        const float smax = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
-        if (smax > R) {
-            shrink = R / (2.0f * smax);
-            R = 2.0f * smax;
-            log2R = __builtin_amdgcn_logf(R);
-        }
+        mt = max_of_halves(max_of_16s(mt));
+        yt = max_of_halves(max_of_16s(yt));
         // the sums are rescaled when a row's maximum has grown past the slack
-        const bool up = mt > m + kSlack;
-        if (__builtin_amdgcn_ballot_w64(up) != 0) {
-            const float m1 = up ? mt : m;
-            const float f = up ? __builtin_amdgcn_exp2f(m - m1) : 1.0f;
-            l *= f;
-            shrink *= f;
+        const bool up_m = mt > m + kSlack, up_y = yt > y + kSlack;
+        if (__builtin_amdgcn_ballot_w64(up_m || up_y) != 0) {
+            const float m1 = up_m ? mt : m, y1 = up_y ? yt : y, f = __builtin_amdgcn_exp2f(y - y1);
+            l *= __builtin_amdgcn_exp2f(m - m1);
             m = m1;
-        }
-        if (__builtin_amdgcn_ballot_w64(shrink != 1.0f) != 0) {
+            y = y1;
+            log2R = y - m;
+            R = __builtin_amdgcn_exp2f(log2R);
 #pragma unroll
             for (int t = 0; t < VD; ++t)
                 for (int e = 0; e < 4; ++e)
-                    o[t][e] *= shrink;
+                    o[t][e] *= f;
         }
         v4i wf[2], wr[2];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             // weights take 2^lv (value scale / R, lifted), sums take it back
-            const float lv = run_shift(__builtin_amdgcn_logf(vs[s]), log2R);
+            const float lv = run_shift(log2s[s], log2R);
             const float back = run_back(R, __builtin_amdgcn_rcpf(vs[s]));
             float p[4];
 #pragma unroll
@@ -643,7 +644,7 @@ __device__ __forceinline__ int swz32(int row)
 //     order in which a lane's weights sit in its registers: chunk 2 u + h of
 //     a row holds tokens 16 u + 4 h + 0..3 and 16 u + 8 + 4 h + 0..3;
 //   * 16-byte chunks of a row swizzled by swz32;
-//   * per run of 16 tokens: score factor, value scale, its log2, its
+//   * per run of 16 tokens: score factor, log2 of the value scale, its
 //     reciprocal.
 // Widen: WAVES waves bring a tile from the cache into LDS, each TPW tokens.
 template <int DT, int D, int WAVES, int TK>
@@ -742,8 +743,8 @@ struct Widen {
         // every wave of a run writes the same scales
         const float sv = held_scale(scale_v);
         if (lane == 0)
-            *(v4f *)(scl + 4 * run) = (v4f){score_factor(scale_k, a.c2), sv, __builtin_amdgcn_logf(sv),
-                                            __builtin_amdgcn_rcpf(sv)};
+            *(v4f *)(scl + 4 * run) = (v4f){score_factor(scale_k, a.c2), __builtin_amdgcn_logf(sv),
+                                            __builtin_amdgcn_rcpf(sv), 0.0f};
     }
 };
 
@@ -853,7 +854,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(D, READY)) void k_attn_rows_m
     for (int t = 0; t < DT32; ++t)
         for (int e = 0; e < 16; ++e)
             o[t][e] = 0.0f;
-    float m = kNothing, l = 0.0f, R = 0.0f, log2R = 0.0f;
+    float m = kNothing, y = kNothing, l = 0.0f, R = 1.0f, log2R = 0.0f;
 
     // LDS offsets of this lane's fragments: chunk 2 s + h of row r32 (and of
     // rows 32, 64, .. further, which swizzle alike) is at place ^ 32 s
@@ -864,19 +865,10 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(D, READY)) void k_attn_rows_m
         constexpr bool MASKED = decltype(masked_tag)::value;
         const uint8_t *sk = lds + buf * kBuf, *sv = sk + kK;
         const float *scl = (const float *)(sk + kTile);
-        v4f sc[NU];
-        float smax = 0.0f;
+        v4f sc[NU];  // of a run: score factor, log2 of the value scale, its reciprocal
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
+        for (int u = 0; u < NU; ++u)
             sc[u] = *(const v4f *)(scl + 4 * u);
-            smax = fmaxf(smax, sc[u][1]);
-        }
-        float shrink = 1.0f;
-        if (smax > R) {
-            shrink = R / (2.0f * smax);
-            R = 2.0f * smax;
-            log2R = __builtin_amdgcn_logf(R);
-        }
         // fragments are read one step ahead of their products; the first ones
         // of the values go out before the softmax
         auto read_k = [&](int s, v4i(&f)[NT]) __attribute__((always_inline)) {
@@ -912,7 +904,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(D, READY)) void k_attn_rows_m
                     x[t][e] = j < sees ? x[t][e] : -INFINITY;
                 }
         }
-        float mt = -INFINITY;
+        float mt = -INFINITY, yt = -INFINITY;
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
             float mu = x[u >> 1][8 * (u & 1)];
@@ -920,31 +912,30 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(D, READY)) void k_attn_rows_m
             for (int e = 1; e < 8; ++e)
                 mu = fmaxf(mu, x[u >> 1][8 * (u & 1) + e]);
             mt = fmaxf(mt, mu * sc[u][0]);
+            yt = fmaxf(yt, __builtin_fmaf(mu, sc[u][0], sc[u][1]));
         }
-        const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mt), __float_as_uint(mt),
-                                                         false, false);
-        mt = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
+        mt = max_of_halves(mt);
+        yt = max_of_halves(yt);
         // the sums are rescaled when a row's maximum has grown past the slack
-        const bool up = mt > m + kSlack;
-        if (__builtin_amdgcn_ballot_w64(up) != 0) {
-            const float m1 = up ? mt : m;
-            const float f = up ? __builtin_amdgcn_exp2f(m - m1) : 1.0f;
-            l *= f;
-            shrink *= f;
+        const bool up_m = mt > m + kSlack, up_y = yt > y + kSlack;
+        if (__builtin_amdgcn_ballot_w64(up_m || up_y) != 0) {
+            const float m1 = up_m ? mt : m, y1 = up_y ? yt : y, f = __builtin_amdgcn_exp2f(y - y1);
+            l *= __builtin_amdgcn_exp2f(m - m1);
             m = m1;
-        }
-        if (__builtin_amdgcn_ballot_w64(shrink != 1.0f) != 0) {
+            y = y1;
+            log2R = y - m;
+            R = __builtin_amdgcn_exp2f(log2R);
 #pragma unroll
             for (int t = 0; t < DT32; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    o[t][e] *= shrink;
+                    o[t][e] *= f;
         }
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
             // weights take 2^b (value scale / R, lifted), sums take it back
-            const float b = run_shift(sc[u][2], log2R) - m;
-            const float back = run_back(R, sc[u][3]);
+            const float b = run_shift(sc[u][1], log2R) - m;
+            const float back = run_back(R, sc[u][2]);
             float p[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)

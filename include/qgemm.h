@@ -423,12 +423,13 @@ qg_status qkv_read(const int8_t *k_codes, const int8_t *v_codes, const float *k_
  * q_heads <= 2^27, seqs * kv_heads <= 2^22, seqs <= 2^20, q_heads <= 65535.
  * Scores are products of dtype operands (codes are exact in both types) with
  * binary32 sums; maxima, sums and outputs are binary32 until the one rounding
- * to dtype at the end.  Softmax weights: sequences of up to 32 rows (new
- * tokens x q_heads / kv_heads) take each as two numbers of dtype; longer ones
- * take each as two numbers of binary16 in binary16 calls and as one in
- * bfloat16 calls, where weights under 2^-24 of a row's largest
- * (times the ratio of value scales) may vanish.  Results are deterministic
- * for the same arguments.
+ * to dtype at the end.  Softmax weights, times their blocks' value scales:
+ * sequences of up to 32 rows (new tokens x q_heads / kv_heads) take each as
+ * two numbers of dtype; longer ones take each as two numbers of binary16 in
+ * binary16 calls and as one, 11 bits, in bfloat16 calls.  Binary16 numbers end
+ * at 2^-30 of the row's largest weight times scale: what is smaller than 2^-31
+ * of it may vanish.  Tokens that a row does not see have no part in its result.
+ * Results are deterministic for the same arguments.
  */
 size_t qattn_kv8_workspace_size(int64_t tokens, int32_t seqs, int32_t max_q, int32_t max_kv,
                                 int32_t q_heads, int32_t kv_heads, int32_t head_dim);

@@ -25,15 +25,16 @@ int main()
             if (!(kc > 0 && std::isfinite(kc) && x == -INFINITY))
                 ++bad, std::printf("score factor %g of %g, %g\n", kc, ks, c2);
         }
-    for (volatile float r : scales)  // R: up to twice a scale met before, or this one's
+    // log2 R: between the least and the largest scale, and the lag of two maxima
+    for (volatile float log2R = -109.0f; log2R <= 108.0f; log2R += 7.75f)
         for (volatile float s : scales) {
-            volatile float h = held_scale(s), R = 2.0f * held_scale(r > s ? r : s);
-            volatile float shift = run_shift(std::log2(h), std::log2(R)), back = run_back(R, 1.0f / h);
-            if (!(h > 0 && std::isfinite(shift) && back > 0 && std::isfinite(back)))
-                ++bad, std::printf("scale %g under %g: %g, %g\n", s, r, shift, back);
-            volatile float both = std::exp2(shift) * back;
-            if (!(std::fabs(both - 1.0f) < 1e-4f))
-                ++bad, std::printf("scale %g under %g: factors give %g\n", s, r, both);
+            volatile float h = held_scale(s), R = std::exp2(log2R);
+            volatile float shift = run_shift(std::log2(h), log2R), back = run_back(R, 1.0f / h);
+            if (!(h > 0 && std::isfinite(shift) && std::isfinite(back)))
+                ++bad, std::printf("scale %g under %g: %g, %g\n", s, R, shift, back);
+            volatile float both = back < 0x1p-126f ? 0.0f : shift + std::log2(back);
+            if (!(std::fabs(both) < 1e-4f))
+                ++bad, std::printf("scale %g under %g: factors give 2^%g\n", s, R, both);
         }
     if (std::fetestexcept(FE_INVALID))
         ++bad, std::printf("an invalid operation\n");

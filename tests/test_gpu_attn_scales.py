@@ -116,6 +116,15 @@ def check(qg, q_lens, kv, Hq, H, D, bs, dtype, scales, causal=True, quiet=None, 
     assert (np.abs(glse[seen] - wlse[seen]) <= e[seen] + 2.0 ** -20 * (1 + np.abs(wlse[seen]))).all()
 
 
+# binary16 results span 2^-24 .. 2^16: scales there are fewer apart
+FAR = {"bf16": (1e-9, 1e9), "f16": (1e-2, 300.0)}
+
+
+def rising(dtype):
+    lo, hi = FAR[dtype]
+    return lambda n: lo * (hi / lo) ** (np.arange(n) / max(1, n - 1))
+
+
 # few rows; many rows, tiles widened on the way; widened ahead (1024 rows and
 # more); each also split over the cache, and sequences in parts
 FORMS = [([2, 1], [500, 400], 4, 2), ([5, 1], [300, 130], 6, 1), ([100, 70], [500, 333], 4, 2),
@@ -126,8 +135,51 @@ FORMS = [([2, 1], [500, 400], 4, 2), ([5, 1], [300, 130], 6, 1), ([100, 70], [50
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("q,kv,Hq,H", FORMS)
+def test_rising_scales(qg, dtype, D, q, kv, Hq, H):
+    """Scales that grow along the sequence: early rows do not see the large ones."""
+    check(qg, q, kv, Hq, H, D, 16, dtype, rising(dtype))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("q,kv,Hq,H", FORMS)
+def test_falling_scales(qg, dtype, q, kv, Hq, H):
+    check(qg, q, kv, Hq, H, 128, 32, dtype, lambda n: rising(dtype)(n)[::-1], causal=False)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q,kv,Hq,H", FORMS)
+def test_large_scales_that_hardly_weigh(qg, dtype, D, q, kv, Hq, H):
+    """Every other block has a value scale far above and a weight of about
+    e^-40: the result is the others'."""
+    big = {"bf16": 2.0 ** 30, "f16": 2.0 ** 14}[dtype]
+    check(qg, q, kv, Hq, H, D, 16, dtype, lambda n: np.where(np.arange(n) % 2, 0.03 * big, 0.03),
+          quiet=lambda i, n: i % 2 == 1)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q,kv,Hq,H", FORMS)
 def test_zero_blocks_first(qg, dtype, D, q, kv, Hq, H):
     """Blocks of zeros (scale 0) before the others: whole tiles in which no
     value scale has been met yet, whose tokens the sum still counts."""
     check(qg, q, kv, Hq, H, D, 16, dtype, lambda n: np.where(np.arange(n) < n * 2 // 3, 0, 0.03))
     check(qg, q, kv, Hq, H, D, 16, dtype, lambda n: np.where(np.arange(n) % 5, 0, 0.03))
+
+
+
+# few rows, many, and many of ready-made tiles
+@pytest.mark.parametrize("q,kv,Hq,H", [([9], [120], 1, 1), ([25], [200], 1, 1), ([16], [150], 2, 1),
+                                       ([200], [200], 2, 2), ([150], [330], 1, 1), ([1100], [1100], 1, 1)])
+def test_steep_scales(qg, q, kv, Hq, H):
+    """Each block's scale 2^12 times the last one's: the new tokens of a wave end
+    in different blocks, and hidden tokens beside theirs have scales far above."""
+    for bs in (16, 32):
+        check(qg, q, kv, Hq, H, 128, bs, "bf16", lambda n: 2.0 ** np.minimum(12.0 * np.arange(n) - 60, 95))
+
+
+def test_scales_at_the_ends_of_their_range(qg):
+    """2^-100 to 2^100, what a cache may hold."""
+    for q, kv, Hq, H in FORMS:
+        check(qg, q, kv, Hq, H, 64, 16, "bf16", lambda n: 2.0 ** np.linspace(-100, 100, n))
+        check(qg, q, kv, Hq, H, 64, 16, "bf16", lambda n: 2.0 ** np.linspace(100, -100, n), causal=False)
