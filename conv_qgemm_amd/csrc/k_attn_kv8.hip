@@ -52,6 +52,7 @@ struct AttnArgs {
     float *po, *pm, *pl;  // partial results of the parts
     uint8_t *images;      // widened tiles (k_attn_widen), or null
     int max_tiles;        // of a sequence
+    int seq0, seq1;       // the sequences that they are of
 };
 
 // A widened tile in memory: what k_attn_rows_many keeps of it in LDS, byte for
@@ -756,7 +757,7 @@ __global__ __launch_bounds__(256) void k_attn_widen(AttnArgs a)
     constexpr int TK = kImageTokens, kTile = 4 * TK * D;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kTile + 64];
     const AttnDesc &d = a.d;
-    const int seq = blockIdx.z, head = blockIdx.y, tile = blockIdx.x;
+    const int seq = a.seq0 + (int)blockIdx.z, head = blockIdx.y, tile = blockIdx.x;
     const int n = (int)min((int64_t)d.b.cu[seq + 1], d.b.tokens) - max(d.b.cu[seq], 0);
     const int len = max(0, min(min(d.b.len[seq], d.b.max_kv), d.c.table_cols * d.c.block_size));
     if ((int64_t)n * a.group <= a.few || tile * TK >= len)
@@ -765,7 +766,7 @@ __global__ __launch_bounds__(256) void k_attn_widen(AttnArgs a)
     w.fetch(tile, w.block_of(tile));
     w.stash(lds, (float *)(lds + kTile));
     __syncthreads();
-    uint8_t *out = a.images + (((int64_t)seq * a.max_tiles + tile) * d.c.heads + head) * image_bytes(D);
+    uint8_t *out = a.images + (((int64_t)blockIdx.z * a.max_tiles + tile) * d.c.heads + head) * image_bytes(D);
     for (int i = threadIdx.x * 16; i < kTile + 64; i += 256 * 16)
         *(v4i *)(out + i) = *(const v4i *)(lds + i);
 }
@@ -823,6 +824,8 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(D, READY)) void k_attn_rows_m
     const Item it = find_item(d.b.cu, d.b.len, d.b.seqs, d.b.tokens, back, G, ROWS, a.extra);
     const int t0 = it.t0, n = it.t1 - t0, row0 = it.index * ROWS;
     if (row0 >= n * G || n * G <= a.few)
+        return;
+    if (READY && (it.seq < a.seq0 || it.seq >= a.seq1))
         return;
     const int len = max(0, min(min(it.len, d.b.max_kv), d.c.table_cols * bs));
     const int first = len - n;
@@ -990,7 +993,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(D, READY)) void k_attn_rows_m
     if (tile0 < tile1) {
         if constexpr (READY) {
             const int64_t step = (int64_t)H * image_bytes(D);
-            const uint8_t *img = a.images + ((int64_t)it.seq * a.max_tiles * H + head) * image_bytes(D);
+            const uint8_t *img = a.images + ((int64_t)(it.seq - a.seq0) * a.max_tiles * H + head) * image_bytes(D);
             auto load = [&](int tile) __attribute__((always_inline)) {
                 const uint8_t *src = img + tile * step;
                 uint8_t *dst = lds + ((tile - tile0) & 1) * kBuf;
@@ -1232,7 +1235,14 @@ constexpr int kShareTokens = 4096;
 //   256 + 500, 32 / 8, D 128: 28 and 33
 //   512 + 8000, 32 / 8, D 128: 129 and 115
 constexpr int kReadyRows = 1024;
-constexpr int64_t kMaxImages = (int64_t)1 << 34;  // bytes
+// They take twice a 16-bit cache's bytes, every sequence as long as max_kv.  Of
+// several, one prompt among decoding steps would make nearly all of that
+// padding: past 64 MB the new tokens must be a quarter of the padded ones (one
+// of 8192 and 127 decoding: 1120 us and no workspace, 1065 and 4.1 GB).  The
+// workspace has room for 1 GB, which slices of the sequences use in turn (64
+// prompts of 4096 to 16384 in 5 slices).
+constexpr int64_t kSmallImages = (int64_t)1 << 26;  // bytes
+constexpr int64_t kMaxImages = (int64_t)1 << 30;
 
 struct Plan {
     int64_t top;    // rows of a sequence, at most
@@ -1240,7 +1250,8 @@ struct Plan {
     bool ready;     // its tiles come widened
     int rows;       // rows of its workgroups
     int max_tiles;
-    int64_t images; // bytes
+    int slice;      // sequences whose widened tiles there is room for at a time
+    int64_t images; // bytes of them
     int splits;
     int shares;
     int64_t part_rows;  // rows of parts
@@ -1255,9 +1266,13 @@ Plan plan(int64_t tokens, int seqs, int max_q, int max_kv, int q_heads, int kv_h
     p.top = (max_q < tokens ? max_q : tokens) * group;
     p.many = p.top > kFew;
     p.max_tiles = (int)(((int64_t)max_kv + kImageTokens - 1) / kImageTokens);
-    const int64_t images = (int64_t)seqs * p.max_tiles * kv_heads * image_bytes(D);
-    p.ready = p.top >= kReadyRows && p.top >= max_kv && images <= kMaxImages && seqs <= 65535;
-    p.images = p.ready ? images : 0;
+    const int64_t image = (int64_t)p.max_tiles * kv_heads * image_bytes(D);  // of a sequence
+    p.ready = p.top >= kReadyRows && p.top >= max_kv && image <= kMaxImages && seqs <= 65535 &&
+              (seqs == 1 || seqs * image <= kSmallImages || (int64_t)seqs * max_kv <= 4 * tokens);
+    if (p.ready) {
+        p.slice = image > 0 && seqs > kMaxImages / image ? (int)(kMaxImages / image) : seqs;
+        p.images = p.slice * image;
+    }
     p.rows = p.ready ? 32 * kReadyWaves : D == 256 ? 128 : 256;
     // Parts per sequence: enough workgroups for the chip, each of 512 tokens
     // or more.  Few rows: one workgroup per compute unit keeps enough bytes in
@@ -1292,11 +1307,14 @@ void launch_rows(const AttnArgs &a, const Plan &p, bool any_few, hipStream_t s)
         const dim3 grid((unsigned)((rows / p.rows + (int64_t)a.extra * d.b.seqs) * d.c.heads),
                         (unsigned)a.splits);
         if (p.ready) {
-            hipLaunchKernelGGL((k_attn_widen<DT, D>),
-                               dim3((unsigned)p.max_tiles, (unsigned)d.c.heads, (unsigned)d.b.seqs),
-                               dim3(256), 0, s, a);
-            hipLaunchKernelGGL((k_attn_rows_many<DT, D, kReadyWaves, true>), grid,
-                               dim3(64 * kReadyWaves), 0, s, a);
+            for (AttnArgs b = a; b.seq0 < d.b.seqs; b.seq0 = b.seq1) {
+                b.seq1 = b.seq0 + p.slice < d.b.seqs ? b.seq0 + p.slice : d.b.seqs;
+                hipLaunchKernelGGL((k_attn_widen<DT, D>),
+                                   dim3((unsigned)p.max_tiles, (unsigned)d.c.heads, (unsigned)(b.seq1 - b.seq0)),
+                                   dim3(256), 0, s, b);
+                hipLaunchKernelGGL((k_attn_rows_many<DT, D, kReadyWaves, true>), grid,
+                                   dim3(64 * kReadyWaves), 0, s, b);
+            }
         } else {
             constexpr int WAVES = D == 256 ? 4 : 8;
             hipLaunchKernelGGL((k_attn_rows_many<DT, D, WAVES, false>), grid, dim3(WAVES * 64), 0, s, a);

@@ -183,3 +183,11 @@ def test_scales_at_the_ends_of_their_range(qg):
     for q, kv, Hq, H in FORMS:
         check(qg, q, kv, Hq, H, 64, 16, "bf16", lambda n: 2.0 ** np.linspace(-100, 100, n))
         check(qg, q, kv, Hq, H, 64, 16, "bf16", lambda n: 2.0 ** np.linspace(100, -100, n), causal=False)
+
+
+def test_a_prompt_among_decoding_steps(qg):
+    """A prompt whose tiles are not widened ahead, for the room that the others
+    would take, beside sequences of the few-row kernel."""
+    for q, kv in (([1100] + [1] * 60, [1100] + [70 + 9 * i for i in range(60)]),
+                  ([1] * 30 + [600, 600], [1 + 19 * i for i in range(30)] + [600, 1190])):
+        check(qg, q, kv, 4, 2, 128, 32, "bf16", lambda n: np.full(n, 0.03))
