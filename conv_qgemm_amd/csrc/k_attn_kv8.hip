@@ -1267,10 +1267,10 @@ Plan plan(int64_t tokens, int seqs, int max_q, int max_kv, int q_heads, int kv_h
     p.many = p.top > kFew;
     p.max_tiles = (int)(((int64_t)max_kv + kImageTokens - 1) / kImageTokens);
     const int64_t image = (int64_t)p.max_tiles * kv_heads * image_bytes(D);  // of a sequence
-    p.ready = p.top >= kReadyRows && p.top >= max_kv && image <= kMaxImages && seqs <= 65535 &&
+    p.ready = max_kv > 0 && p.top >= kReadyRows && p.top >= max_kv && image <= kMaxImages && seqs <= 65535 &&
               (seqs == 1 || seqs * image <= kSmallImages || (int64_t)seqs * max_kv <= 4 * tokens);
     if (p.ready) {
-        p.slice = image > 0 && seqs > kMaxImages / image ? (int)(kMaxImages / image) : seqs;
+        p.slice = seqs > kMaxImages / image ? (int)(kMaxImages / image) : seqs;
         p.images = p.slice * image;
     }
     p.rows = p.ready ? 32 * kReadyWaves : D == 256 ? 128 : 256;
