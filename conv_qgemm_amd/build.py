@@ -4,8 +4,9 @@ The library's HIP sources under ``csrc/`` are compiled to objects in
 parallel and linked into ``conv_qgemm_amd/libqgemm.so``; the benchmark's
 calibration kernels (``csrc/calib.hip``) go to their own
 ``conv_qgemm_amd/libqgcalib.so``; the Python callables of the decoding
-step's entry points (host code only, for the torch that it is built with) to ``conv_qgemm_amd/_qcall.so``.  Objects go to ``_build/`` at the
-repository root.
+step's entry points (host code only, for the torch that it is built with) to
+``conv_qgemm_amd/_qcall.so``.  Objects go to ``_build/`` at the repository
+root.
 """
 from __future__ import annotations
 
@@ -110,11 +111,11 @@ def build(verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs), 8)) as ex:
         call = ex.submit(_build_call, verbose)
         objs = list(ex.map(_compile, srcs))
-        call.result()
     n, c = len(SOURCES), len(CALIB_SOURCES)
     _link(objs[:n], LIB, verbose)
     _link(objs[n:n + c], CALIB_LIB, verbose)
     _link(objs[n + c:], VENDOR_LIB, verbose, libs=["-L/opt/rocm/lib", "-lhipblaslt"])
+    call.result()  # a failure there leaves the libraries linked
     return LIB
 
 

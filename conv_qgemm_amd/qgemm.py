@@ -3,7 +3,8 @@
 Argument marshalling only: torch tensors on the GPU give device pointers,
 leading dimensions and the current stream; every step of the computation runs
 in the library's HIP kernels.  If ``libqgemm.so`` is missing or cannot be
-loaded, importing this module raises -- there is no fallback path.
+loaded, importing this module raises -- there is no fallback path.  The int8
+attention layer's functions also need ``_qcall.so`` and raise without it.
 
 Layouts follow ``include/qgemm.h``: A ``[M][K]`` row-major, B ``[N][K]``
 (column-major K x N), packed int4 operands as ``uint8`` ``[rows][K/2]`` with
@@ -108,14 +109,25 @@ def _load():
     return lib
 
 
+class _NoCalls:
+    """In the place of the module that is missing: the first use says so."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError("conv_qgemm_amd/_qcall.so is not built for this Python and torch; run "
+                          "__graft_entry__.build() (or python conv_qgemm_amd/build.py)") from self._why
+
+
 def _load_calls():
     """The library's calls of one decoding step without ctypes' conversions
-    (`lib` has them too)."""
+    (`lib` has them too).  The int8 attention layer's functions need it, the
+    others only `lib`."""
     try:
         from conv_qgemm_amd import _qcall
     except ImportError as e:
-        raise ImportError("conv_qgemm_amd/_qcall.so is not built; run __graft_entry__.build() "
-                          "(or python conv_qgemm_amd/build.py)") from e
+        return _NoCalls(e)
     for name in ("qgemm_s8s8_dequant", "qkv_append_rope", "qkv_read", "qattn_kv8_workspace_size",
                  "qattn_kv8"):
         _qcall.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
