@@ -60,17 +60,18 @@ HBM_BOUND = ("w4a8", "w4a8_m64", "quant_a8", "dw3x3")
 # buffer sets per workload so that the rotation exceeds the Infinity Cache
 ROTATE = {"pointwise": 1, "s4s4": 7, "conv3x3": 40, "conv3x3_zp": 40, "dw3x3": 40,
           "quant_a8": 3, "w4a8": 5, "w4a8_m64": 5, "w4a8_prefill": 3, "s8s8": 3, "s8s8_zp": 3}
+RING = ("conv_qgemm_amd/csrc/k_gemm_dma.hip", "conv_qgemm_amd/csrc/gemm_ring.hpp")
 KERNEL_SOURCES = {
-    "s8s8": "conv_qgemm_amd/csrc/gemm_ring.hpp",
-    "s4s4": "conv_qgemm_amd/csrc/gemm_ring.hpp",
+    "s8s8": RING,
+    "s4s4": RING,
     "pointwise": "conv_qgemm_amd/csrc/k_tile_gemm.hip",
     "conv3x3": "conv_qgemm_amd/csrc/k_conv_halo.hip",
     "w4a8": "conv_qgemm_amd/csrc/k_skinny_w4a8.hip",
     "w4a8_m64": "conv_qgemm_amd/csrc/k_skinny_w4a8.hip",
     "dw3x3": "conv_qgemm_amd/csrc/k_dwconv.hip",
     "quant_a8": "conv_qgemm_amd/csrc/k_quant.hip",
-    "s8s8_zp": "conv_qgemm_amd/csrc/gemm_ring.hpp",
-    "w4a8_prefill": "conv_qgemm_amd/csrc/gemm_ring.hpp",
+    "s8s8_zp": RING,
+    "w4a8_prefill": RING,
     "conv3x3_zp": "conv_qgemm_amd/csrc/k_conv_halo.hip",
 }
 
@@ -140,11 +141,12 @@ def code_text(src):
     return " ".join("".join(out).split())
 
 
-def src_sha(path):
-    """Fingerprint of a kernel's code (its source and the shared device
-    header, comments and layout aside)."""
+def src_sha(sources):
+    """Fingerprint of a kernel's code (its source or sources and the shared
+    device header, comments and layout aside)."""
     h = hashlib.sha256()
-    for p in (path, "conv_qgemm_amd/csrc/dev_common.hpp"):
+    sources = (sources,) if isinstance(sources, str) else sources
+    for p in (*sources, "conv_qgemm_amd/csrc/dev_common.hpp"):
         with open(os.path.join(ROOT, p), encoding="utf-8") as f:
             h.update(code_text(f.read()).encode())
     return h.hexdigest()[:16]
