@@ -349,11 +349,14 @@ qg_status qgemm_s8s8_dequant(const int8_t *A, int64_t lda, const int8_t *B, int6
  * q_heads a multiple of kv_heads, both >= 1; every base pointer 16-byte
  * aligned (block_table, cu_seqlens, kv_lens: 4-byte); rows of new tokens
  * have dense heads and strides (in elements) that are multiples of 16 bytes.
+ * Sequences may share blocks (a common prefix), except for those that
+ * qkv_append_rope writes to.  Limits of all calls: tokens and table_cols *
+ * block_size <= 2^30, seqs <= 2^20, q_heads and kv_heads <= 65535.
  * Device-resident preconditions, not checked by the library: the two arrays
  * of lengths as above, block numbers in [0, num_blocks) for every token
- * that a call touches, no block twice; scales 0 (of all-zero codes) or in
- * [2^-100, 2^100].  Outside them the outputs are unspecified; the kernels
- * ignore block numbers, tokens and table columns out of range (no fault).
+ * that a call touches; scales 0 (of all-zero codes) or in [2^-100, 2^100].
+ * Outside them the outputs are unspecified; the kernels ignore block numbers,
+ * tokens and table columns out of range (no fault).
  */
 
 /*
@@ -379,6 +382,8 @@ qg_status qgemm_s8s8_dequant(const int8_t *A, int64_t lda, const int8_t *B, int6
  * Values are finite.  A block whose largest new value / 127 is below 2^-100
  * counts that value as 0 (its new codes are those of the scale it has).
  * Codes of a block's places past the sequence's length are not written.
+ * No block that a call writes to may be in two of its sequences.  Limit:
+ * (tokens / block_size + 2 * seqs) * kv_heads * 2 + tokens < 2^24.
  */
 qg_status qkv_append_rope(const void *Q, int64_t ldq, const void *K, int64_t ldk, const void *V,
                           int64_t ldv, int32_t dtype, const float *cos_sin, int32_t rot_dim,
@@ -396,6 +401,7 @@ qg_status qkv_append_rope(const void *Q, int64_t ldq, const void *K, int64_t ldk
  *   start int32 [seqs]; cu_out int32 [seqs + 1], running sums, `tokens` last
  *   K_out, V_out [tokens][kv_heads][head_dim] dense, of dtype:
  *         T(code * scale), the product rounded to binary32, then to T
+ * Limit: tokens < 2^24.
  */
 qg_status qkv_read(const int8_t *k_codes, const int8_t *v_codes, const float *k_scale,
                    const float *v_scale, int64_t num_blocks, int32_t block_size,
@@ -419,8 +425,9 @@ qg_status qkv_read(const int8_t *k_codes, const int8_t *v_codes, const float *k_
  *         seqs, max_q, max_kv and heads, 16-byte aligned; NULL when that is 0.
  *         Nothing is kept there between calls; calls that share one must be
  *         ordered (one stream).
- * Tokens of a sequence at or past max_kv are not looked at.  Limits: tokens *
- * q_heads <= 2^27, seqs * kv_heads <= 2^22, seqs <= 2^20, q_heads <= 65535.
+ * A length above max_kv is taken as max_kv.  Limits, with r = tokens * q_heads /
+ * kv_heads rows: tokens * q_heads <= 2^30, (r / 16 + seqs) * kv_heads < 2^24,
+ * (r / 128 + seqs) * kv_heads < 2^23.
  * Scores are products of dtype operands (codes are exact in both types) with
  * binary32 sums; maxima, sums and outputs are binary32 until the one rounding
  * to dtype at the end.  Softmax weights, times their blocks' value scales:
