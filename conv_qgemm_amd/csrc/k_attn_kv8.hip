@@ -784,9 +784,9 @@ __global__ __launch_bounds__(256) void k_attn_widen(AttnArgs a)
 // step; tiles of 32 tokens leave room for three (D = 128) or four (64).
 // Otherwise 8 waves widen each tile of 64 once for 256 rows.
 //
-// Measured: a prompt of 8192 tokens, 32 / 8 heads of 128, causal, READY: 546 to
-// 564 us by board (13 of them k_attn_widen), 550 GFLOP, 0.98 to 1.0 PFLOP/s.
-// The matrix cores are busy 54% of the cycles, the softmax's and the scales'
+// Measured: a prompt of 8192 tokens, 32 / 8 heads of 128, causal, READY: 555 to
+// 585 us by board (14 of them k_attn_widen), 550 GFLOP, 0.94 to 0.99 PFLOP/s.
+// The matrix cores are busy 53% of the cycles, the softmax's and the scales'
 // vector work most of the rest (alone it takes 219 us), and the clock settles
 // at 1.8 GHz; a large bfloat16 product on this card reaches 1.41 PFLOP/s.
 constexpr int kReadyWaves = 4;
@@ -805,8 +805,8 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(D, READY)) void k_attn_rows_m
     // A weight's rounding to binary16 is an eighth of the rounding of a
     // bfloat16 result but as large as that of a binary16 one (error against 64
     // bits 0.00037, the result's own rounding 0.00021): there a second product
-    // takes its rest.  It costs a binary16 prompt of 8192 tokens 190 us, 837
-    // instead of 647.
+    // takes its rest.  It costs a binary16 prompt of 8192 tokens 190 us (837
+    // instead of 647 on one board; 776 on another, bfloat16 584).
     constexpr bool REST = DT == DT_F16;
     constexpr float kSlack = 8.0f;  // a maximum may lag by 2^8 before the sums are rescaled
     __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kBuf];

@@ -519,11 +519,14 @@ hipError_t run_dequant(const DequantDesc &d, hipStream_t s)
         return run_tile<DT, 32, 32, 2, 4, 4>(a, s);
     if (d.M <= 64)
         return run_stream<DT, 2>(a, d.cus, s);
-    // The tile by what fills the chip's 256 compute units once (us, weights
-    // from memory, HIP graph; M x N x K):
-    //   128x128 tiles fill it: 512x8192x8192 56.7, with one group of waves 59.6
+    // The tile by what fills the chip's 256 compute units (us, weights from
+    // memory, HIP graph; M x N x K):
+    //   256 tiles of 128x128 fill it: 512x8192x8192 56.7, with one group of
+    //   waves 59.6
     //   128x64 where 64x64 would need a second round: 333x4107x4112 21.6
-    //   against 26.7; 512x4096x4096 20.9 against 24.5
+    //   against 26.7; 512x4096x4096 20.9 against 24.5.  From 129 to 255 tiles of
+    //   128x128 it has more than 256 itself and takes two rounds, which has not
+    //   been measured against one of 128x128
     //   64x64: 256x4096x4096 12.9 against 17.2 with 128x64
     //   64x32 when even those leave half of it idle: 70x2900x2064 6.7
     //   against 7.9 with 64x64

@@ -185,7 +185,7 @@ __device__ __forceinline__ v2u code8(const float (&x)[8], float sc, float rsc, b
 // once and every code written once.  The workgroups past those of the blocks
 // rotate queries, so that a step is one launch.  Bound by memory when there
 // are many tokens (6 prompts of up to 4099 tokens, 16 heads of 64, binary16,
-// queries included: 43 us, 182 MB, 4.2 TB/s; a copy reaches 4.45), by three
+// queries included: 43 us, 182 MB, 4.2 TB/s; a 1 GiB copy reaches 5.1), by three
 // dependent loads (sums, block number, scale) when there are few (48 new
 // tokens: 6.5 us).
 template <int DT, int U, bool BOTH>
