@@ -13,8 +13,8 @@
 // with R = 2^(y - m).  So w stays within [0, 1] and the row's largest term is
 // near 1: what a weight loses to binary16's range is small beside the row's own
 // terms, whatever scales other rows or hidden tokens have.  (One R for a wave,
-// at least every scale met, was as fast but let a row vanish beside a later
-// block's scale.)
+// at least every scale met, was 1.5% faster on a prompt but let a row vanish
+// beside a later block's scale.)
 //
 // The product K Q^T leaves token x row tiles in the layout that the second
 // product, V^T W^T, takes its weights in (a lane holds 4 tokens of one row

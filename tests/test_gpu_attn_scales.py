@@ -191,3 +191,30 @@ def test_a_prompt_among_decoding_steps(qg):
     for q, kv in (([1100] + [1] * 60, [1100] + [70 + 9 * i for i in range(60)]),
                   ([1] * 30 + [600, 600], [1 + 19 * i for i in range(30)] + [600, 1190])):
         check(qg, q, kv, 4, 2, 128, 32, "bf16", lambda n: np.full(n, 0.03))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("n,L,Hq,H,D", [(16, 100, 2, 2, 128), (20, 90, 1, 1, 64), (60, 150, 4, 2, 128),
+                                        (300, 300, 4, 1, 64), (1100, 1100, 1, 1, 128), (40, 2100, 2, 1, 256)])
+def test_hidden_tokens_have_no_part(qg, dtype, n, L, Hq, H, D):
+    """Other codes and scales in the blocks that a new token does not see leave
+    its bits alone."""
+    rng = np.random.default_rng(9)
+    bs, blocks = 16, -(-L // 16)
+    cache = as_cache(qg, make_cache(rng, blocks, H, bs, D))
+    table = dev(np.arange(blocks, dtype=np.int32)[None])
+    q = torch.from_numpy(rng.normal(size=(n, Hq, D))).to(DTYPES[dtype]).cuda()
+    args = (table, dev(np.array([0, n], np.int32)), dev(np.array([L], np.int32)), n, L)
+    print(f"hidden tokens {n} of {L}, {Hq}/{H} heads of {D} {dtype}", flush=True)
+    first = qg.qattn_kv8(q, cache, *args, return_lse=True)
+    cut = L - n // 2  # tokens from here on are others
+    b0 = -(-cut // bs)
+    sees = b0 * bs - (L - n)  # new tokens that see only blocks before b0
+    assert 0 < sees < n
+    for scale in (2.0 ** 60, 0.0):
+        for t in cache[:2]:
+            t[b0:] = torch.randint(-127, 128, t[b0:].shape, dtype=torch.int8, device="cuda") if scale else 0
+        for t in cache[2:]:
+            t[b0:] = scale
+        again = qg.qattn_kv8(q, cache, *args, return_lse=True)
+        assert torch.equal(first[0][:sees], again[0][:sees]) and torch.equal(first[1][:sees], again[1][:sees])
